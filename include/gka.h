@@ -420,7 +420,7 @@ gka_status gka_join_bwd(const gka_join_params* p, const void* res, const void* y
  * The gate is given by its logit: near gamma = 1 a 16-bit gamma could not hold how long the
  * memory is, while the logit keeps 1 - gamma to its relative precision. f = +inf keeps the state
  * (with complement = 1 the token writes nothing: padding), f = -inf drops it (the first token of
- * a document in a packed row).
+ * a document in a packed row; a state that is not finite leaves NaN, as 0 times infinity does).
  *   B, T, C      batch rows, tokens, channels: B >= 1, T >= 0, C >= 1, B C <= 2^30
  *   x_bstride, x_tstride, f_bstride, f_tstride   elements from one batch row / token to the next;
  *                a token stride covers C, and 256 of them stay below 2^31 bytes; a batch stride

@@ -22,6 +22,14 @@
 // precision; a thread keeps v = copysign(s, f) and takes the larger one as 1 - s, rounded to nearest
 // (a bias in gamma near 1 would grow with the memory's length).
 //
+// Infinities go as gamma h + beta x takes them. The forms above turn an infinity into NaN at the next step
+// (s (x - h) + h is inf - inf), and x - h overflows where h itself does not; but what is not finite stays
+// so in them. A slice whose end is not finite is therefore run again, each step that is not finite in the
+// definition's form; finite channels keep their bits. A product of gates that underflows is kept above
+// zero, since an infinite state survives it, while a gate of zero times infinity is NaN. The checks cost a
+// finite call up to 1 % forward and 1 to 2 % backward (4 sequences of 8192 steps by 2048 channels: 133 us
+// without, 136 with them).
+//
 // Measured (bf16): 4 sequences of 8192 steps by 2048 channels 90 us forward (4.5 TB/s) and 133 us
 // backward (5.0 TB/s); one of 131072 steps by 1024 channels 180 us (4.5 TB/s) and 315 us (4.3 TB/s).
 // The card copies 5.1 TB/s; what is between is the start of a workgroup (counter, loads, scan,
@@ -81,14 +89,61 @@ inline auto with_backward(int dtype, int B, int T, int C, Fn fn) {
 // v = copysign(min(gamma, 1 - gamma), f); f >= 0 (and +0) exactly when v's sign bit is clear
 __device__ inline float gate_of(float f) { return __builtin_copysignf(sigmoids(f).small, f); }
 __device__ inline bool keeps(float v) { return (int)__float_as_uint(v) >= 0; }
-// gamma a, with one rounding
-__device__ inline float times_gamma(float v, float a) { return fmaf(-v, a, keeps(v) ? a : 0.0f); }
+// v's sign in every bit, and the choice by it: one operation each and no condition mask, which the compiler
+// would hold in scalar registers for every element, or wait for. In assembly, since it would make a
+// comparison of them again.
+__device__ inline uint32_t sign_of(float v) {
+  uint32_t m;
+  asm volatile("v_ashrrev_i32 %0, 31, %1" : "=v"(m) : "v"(v));
+  return m;
+}
+__device__ inline float pick(uint32_t m, float clear, float set) {
+  float r;
+  asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(r) : "v"(m), "v"(set), "v"(clear));
+  return r;
+}
+__device__ inline float if_clear(uint32_t m, float a) {
+  float r;
+  asm("v_bfi_b32 %0, %1, 0, %2" : "=v"(r) : "v"(m), "v"(a));
+  return r;
+}
+__device__ inline float if_set(uint32_t m, float a) { return __uint_as_float(m & __float_as_uint(a)); }
+// gamma a, with one rounding; m = sign_of(v)
+__device__ inline float times_gamma(float v, uint32_t m, float a) { return fmaf(-v, a, if_clear(m, a)); }
 // (1 - gamma) a, with one rounding
-__device__ inline float times_omg(float v, float a) { return fmaf(v, a, keeps(v) ? 0.0f : a); }
+__device__ inline float times_omg(float v, uint32_t m, float a) { return fmaf(v, a, if_set(m, a)); }
 // one step: gamma h + (1 - gamma) x = the nearer of h and x plus s times the way to the other
 template <bool COMP>
-__device__ inline float advance(float v, float h, float x) {
-  return COMP ? fmaf(v, x - h, keeps(v) ? h : x) : times_gamma(v, h) + x;
+__device__ inline float advance(float v, uint32_t m, float h, float x) {
+  return COMP ? fmaf(v, x - h, pick(m, h, x)) : times_gamma(v, m, h) + x;
+}
+
+// The same with infinities as IEEE arithmetic has them in gamma a, (1 - gamma) a and gamma h + beta x, and
+// without an x - h that overflows. Steps whose result is finite have the bits of the forms above.
+__device__ inline bool finite(float a) { return __builtin_isfinite(a); }
+__device__ inline float rest_of(float s, float a) {  // (1 - s) a, s <= 1/2
+  return fmaf(-s, fminf(fmaxf(a, -3.40282347e38f), 3.40282347e38f), a);
+}
+__device__ inline float times_gamma_ieee(float v, float a) {
+  const float r = times_gamma(v, sign_of(v), a), s = fabsf(v);
+  return finite(r) ? r : keeps(v) ? rest_of(s, a) : s * a;
+}
+__device__ inline float times_omg_ieee(float v, float a) {
+  const float r = times_omg(v, sign_of(v), a), s = fabsf(v);
+  return finite(r) ? r : keeps(v) ? s * a : rest_of(s, a);
+}
+template <bool COMP>
+__device__ inline float advance_ieee(float v, float h, float x) {
+  const float r = advance<COMP>(v, sign_of(v), h, x), s = fabsf(v);
+  if (finite(r)) return r;
+  if (!COMP) return times_gamma_ieee(v, h) + x;
+  return keeps(v) ? fmaf(s, x, rest_of(s, h)) : fmaf(s, h, rest_of(s, x));
+}
+// A h + H of a run whose product of gates A may have underflown: an infinite h survives gates that are not
+// zero (`zero`: one of them is)
+__device__ inline float kept(float A, bool zero) { return A == 0.0f && !zero ? __uint_as_float(1u) : A; }
+__device__ inline float run_end(float A, float h, float H, bool zero) {
+  return fmaf(finite(h) ? A : kept(A, zero), h, H);
 }
 
 // Channels: a tile's group of VEC channels that would pass C starts at C - VEC instead, so any C >= VEC
@@ -128,6 +183,99 @@ __device__ inline void slice_gates(const vec_t<T, VEC> (&f)[L], int rows, bool t
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v[l][i] = l < rows ? v[l][i] : 0.0f;
   }
+}
+
+// Where a thread's vectors lie: VEC channels from c0 on (its own from `nominal` on) of L steps from step t0
+// of the segment on, of which `rows` steps are left before the segment's end. lane_again derives it a second
+// time, so that it need not be held in registers meanwhile.
+struct Lane {
+  int cg, ts, nominal, c0, rows;
+  uint32_t t0;
+};
+template <typename S>
+__device__ inline Lane lane_of(uint32_t tid, int tile, int C, int trows) {
+  Lane q;
+  q.cg = tid % S::NCG;
+  q.ts = tid / S::NCG;
+  q.nominal = tile * S::CT + q.cg * S::VEC;
+  q.c0 = group_start<S::VEC>(q.nominal, C);
+  q.t0 = (uint32_t)(q.ts * S::L);
+  q.rows = trows - q.ts * S::L;
+  return q;
+}
+template <typename S>
+__device__ inline Lane lane_again(int tile, int C, int trows) {
+  uint32_t tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return lane_of<S>(tid, tile, C, trows);
+}
+// The gates for a rare path: what it needs of them the compiler derives there, instead of before the branch
+template <int VEC, int L>
+struct Again {
+  float v[L][VEC];
+  __device__ inline explicit Again(const float (&from)[L][VEC]) {
+#pragma unroll
+    for (int l = 0; l < L; ++l)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        v[l][i] = from[l][i];
+        asm volatile("" : "+v"(v[l][i]));
+      }
+  }
+};
+
+// The slice's pairs (A, H) and, with GRAD, G. Marks the slice in the masks of the channels that have a gate
+// of zero in it.
+template <bool COMP, bool GRAD, typename T, int VEC, int L>
+__device__ inline void slice_pairs(const float (&v)[L][VEC], const vec_t<T, VEC> (&x)[L],
+                                   const vec_t<T, VEC> (&dh)[L], float (&A)[VEC], float (&H)[VEC],
+                                   float (&G)[VEC], uint32_t* zeros, int ts) {
+  float odd = 0.0f, least = 1.0f;  // NaN where an H or G is not finite; 0 where an A is
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    A[i] = 1.0f;
+    H[i] = G[i] = 0.0f;
+#pragma unroll
+    for (int l = 0; l < L; ++l) {
+      const uint32_t m = sign_of(v[l][i]);
+      A[i] = times_gamma(v[l][i], m, A[i]);
+      H[i] = advance<COMP>(v[l][i], m, H[i], (float)x[l][i]);
+      if (GRAD) G[i] = fmaf(A[i], (float)dh[l][i], G[i]);
+    }
+    odd = fmaf(H[i], 0.0f, odd);
+    if (GRAD) odd = fmaf(G[i], 0.0f, odd);
+    least = fminf(least, A[i]);
+  }
+  if (__builtin_expect(least + odd > 0.0f, 1)) return;
+  const Again<VEC, L> g(v);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    if (A[i] == 0.0f) {
+      bool zero = false;
+#pragma unroll
+      for (int l = 0; l < L; ++l) zero |= __float_as_uint(g.v[l][i]) == 0x80000000u;
+      A[i] = kept(A[i], zero);
+      if (zero) atomicOr(zeros + i, 1u << ts);
+    }
+    if (!finite(H[i])) {
+      H[i] = 0.0f;
+#pragma unroll
+      for (int l = 0; l < L; ++l) H[i] = advance_ieee<COMP>(g.v[l][i], H[i], (float)x[l][i]);
+    }
+    if (GRAD && !finite(G[i])) {
+      G[i] = 0.0f;
+#pragma unroll
+      for (int l = L - 1; l >= 0; --l) G[i] = times_gamma_ieee(g.v[l][i], (float)dh[l][i] + G[i]);
+    }
+  }
+}
+// (0 times an infinity is NaN)
+template <int VEC>
+__device__ inline bool all_finite(const float (&h)[VEC]) {
+  float odd = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) odd = fmaf(h[i], 0.0f, odd);
+  return odd == 0.0f;
 }
 
 __device__ inline void publish(uint64_t* word, uint32_t status, float low) {
@@ -178,7 +326,8 @@ __device__ inline float look_back(const uint64_t* at) {
 struct Spot {
   int chain, b, tile, u;
 };
-__device__ inline Spot take_spot(const RecurArgs& a, bool near, int* lds) {
+__device__ inline Spot take_spot(const RecurArgs& a, bool near, int* lds, uint32_t* zeros,
+                                 int channels) {
   Spot p;
   // Every argument is read at the start, in one round trip, not in a second one after the counter's: 8
   // sequences of 2048 steps by 1024 channels 23.5 us forward, 25.1 without.
@@ -190,10 +339,11 @@ __device__ inline Spot take_spot(const RecurArgs& a, bool near, int* lds) {
   p.b = p.chain / a.tiles;
   p.tile = p.chain % a.tiles;
   p.u = 0;
-  if (a.S > 1) {
-    if (threadIdx.x == 0) *lds = (int)atomicAdd(a.tickets + p.chain, 1u);
+  if (a.S > 1 || a.state_in) {  // (a start of zeros needs no masks)
+    if (threadIdx.x < channels) zeros[threadIdx.x] = 0;
+    if (a.S > 1 && threadIdx.x == 0) *lds = (int)atomicAdd(a.tickets + p.chain, 1u);
     lds_barrier();
-    p.u = __builtin_amdgcn_readfirstlane(*lds);  // uniform: the segment's addresses are scalar
+    if (a.S > 1) p.u = __builtin_amdgcn_readfirstlane(*lds);  // uniform: scalar addresses of the segment
   }
   return p;
 }
@@ -212,11 +362,12 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
   constexpr int VEC = S::VEC, L = S::L, CT = S::CT, NCG = S::NCG, NTS = S::NTS, SEG = S::SEG;
   __shared__ float sA[NTS][CT], sH[NTS][CT], start[CT];
   __shared__ int ticket;
-  const Spot p = take_spot(a, (uint32_t)a.C * sizeof(T) % 128 != 0, &ticket);
-  const int cg = threadIdx.x % NCG, ts = threadIdx.x / NCG;
-  const int nominal = p.tile * CT + cg * VEC, c0 = group_start<VEC>(nominal, a.C);
-  const int tseg = p.u * SEG;
-  const int trows = min(SEG, a.T - tseg), rows = trows - ts * L;  // of the segment, from the slice
+  __shared__ uint32_t zeros[CT];  // per channel, a bit for every slice with a gate of zero
+  static_assert(NTS <= 32, "one bit per slice");
+  const Spot p = take_spot(a, (uint32_t)a.C * sizeof(T) % 128 != 0, &ticket, zeros, CT);
+  const int tseg = p.u * SEG, trows = min(SEG, a.T - tseg);
+  const Lane q = lane_of<S>(threadIdx.x, p.tile, a.C, trows);
+  const int cg = q.cg, ts = q.ts, c0 = q.c0;
   // the channel that a scanning thread (of the first CT) takes, and its initial state: in its register
   // before the barrier, since the owner's wave may write the final one after it
   const int group = p.tile * CT + (int)threadIdx.x / VEC * VEC;
@@ -225,26 +376,24 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
   float h0 = 0.0f;
   vec_t<T, VEC> x[L];
   float v[L][VEC];
+  const auto rf = segment_buffer<T>(a.f, p.b * a.fb + tseg * a.ft, a.ft, trows, a.C);
+  const auto rx = segment_buffer<T>(a.x, p.b * a.xb + tseg * a.xt, a.xt, trows, a.C);
   {
     vec_t<T, VEC> f[L];
-    const auto rf = segment_buffer<T>(a.f, p.b * a.fb + tseg * a.ft, a.ft, trows, a.C);
-    const auto rx = segment_buffer<T>(a.x, p.b * a.xb + tseg * a.xt, a.xt, trows, a.C);
-    load_slice<T, VEC, L>(rf, (uint32_t)(ts * L) * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
-    load_slice<T, VEC, L>(rx, (uint32_t)(ts * L) * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
+    load_slice<T, VEC, L>(rf, q.t0 * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
+    load_slice<T, VEC, L>(rx, q.t0 * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
     if (p.u == 0 && a.state_in && threadIdx.x < CT && group < a.C)
       h0 = a.state_in[(int64_t)p.b * a.C + c];
-    slice_gates<T, VEC, L>(f, rows, trows < SEG, v);
+    slice_gates<T, VEC, L>(f, q.rows, trows < SEG, v);
   }
+  {
+    float A[VEC], H[VEC], none[VEC];
+    slice_pairs<COMP, false, T, VEC, L>(v, x, x, A, H, none, zeros + cg * VEC, ts);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float A = 1.0f, H = 0.0f;
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      A = times_gamma(v[l][i], A);
-      H = advance<COMP>(v[l][i], H, (float)x[l][i]);
+    for (int i = 0; i < VEC; ++i) {
+      sA[ts][cg * VEC + i] = A[i];
+      sH[ts][cg * VEC + i] = H[i];
     }
-    sA[ts][cg * VEC + i] = A;
-    sH[ts][cg * VEC + i] = H;
   }
   asm volatile("" : "+v"(h0));
   lds_barrier();
@@ -259,6 +408,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
       Ht = fmaf(Ak, Ht, Hk);
       At *= Ak;
     }
+    const uint32_t zero = zeros[threadIdx.x];
+    At = kept(At, zero != 0);
     uint64_t* word = a.words + ((int64_t)p.chain * a.S + p.u) * CT + threadIdx.x;
     const bool last = p.u == a.S - 1;
     float h = h0;
@@ -282,33 +433,55 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
         const int s = p.u * PER + j;
         if (s < n)
           a.carry[((int64_t)p.b * n + s) * a.C + c] =
-              fmaf(sA[j * every][threadIdx.x], h, sH[j * every][threadIdx.x]);
+              run_end(sA[j * every][threadIdx.x], h, sH[j * every][threadIdx.x],
+                      (zero & ((1u << j * every) - 1)) != 0);
       }
     }
   }
   lds_barrier();
-  if (nominal >= a.C) return;
-  float h[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    h[i] = fmaf(sA[ts][cg * VEC + i], start[cg * VEC + i], sH[ts][cg * VEC + i]);
+  const Lane o = lane_again<S>(p.tile, a.C, trows);
+  if (o.nominal >= a.C) return;
   const auto rh = segment_buffer<T>(a.h, ((int64_t)p.b * a.T + tseg) * a.C, a.C, trows, a.C);
-  const uint32_t off = (uint32_t)(ts * L) * (uint32_t)a.C + c0;
   // A tile of fewer than VEC channels has one group, which starts in the tile before. The state that it
   // read for that one's channels may be their final one already, so it stores its own channels alone.
   const bool crossing = VEC > 1 && p.tile * CT + VEC > a.C;
-#pragma unroll
-  for (int l = 0; l < L; ++l) {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) h[i] = advance<COMP>(v[l][i], h[i], (float)x[l][i]);
-    const uint32_t at = (off + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
+  auto store = [&](const Lane& k, int l, const float(&h)[VEC]) {
+    const uint32_t at = (k.t0 * (uint32_t)a.C + k.c0 + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
     if (!crossing) {
       buffer_store_vec<T, VEC>(rh, at, h);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (c0 + i >= nominal) buffer_store_vec<T, 1>(rh, at + (uint32_t)i * (uint32_t)sizeof(T), {h[i]});
+        if (k.c0 + i >= k.nominal)
+          buffer_store_vec<T, 1>(rh, at + (uint32_t)i * (uint32_t)sizeof(T), {h[i]});
     }
+  };
+  float h[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i)
+    h[i] = fmaf(sA[o.ts][o.cg * VEC + i], start[o.cg * VEC + i], sH[o.ts][o.cg * VEC + i]);
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = advance<COMP>(v[l][i], sign_of(v[l][i]), h[i], (float)x[l][i]);
+    store(o, l, h);
+  }
+  if (__builtin_expect(all_finite(h), 1)) return;
+  // again, over what was stored: a loop that reads f and x once more, since holding them would spill
+  const Lane k = lane_again<S>(p.tile, a.C, trows);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    const int c = k.cg * VEC + i;
+    h[i] = run_end(sA[k.ts][c], start[c], sH[k.ts][c], (zeros[c] & ((1u << k.ts) - 1)) != 0);
+  }
+#pragma unroll 1
+  for (int l = 0; l < min(L, k.rows); ++l) {
+    const uint32_t t = k.t0 + (uint32_t)l;
+    const auto f = buffer_load_vec<T, VEC>(rf, (t * (uint32_t)a.ft + k.c0) * (uint32_t)sizeof(T));
+    const auto xl = buffer_load_vec<T, VEC>(rx, (t * (uint32_t)a.xt + k.c0) * (uint32_t)sizeof(T));
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = advance_ieee<COMP>(gate_of((float)f[i]), h[i], (float)xl[i]);
+    store(k, l, h);
   }
 }
 
@@ -323,14 +496,14 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
   // the slices right of each
   __shared__ float sA[NTS][CT], sH[NTS][CT], sG[NTS][CT], sR[NTS][CT], rin[CT];
   __shared__ int ticket;
-  const Spot p = take_spot(a, true, &ticket);
+  __shared__ uint32_t zeros[CT];  // per channel, a bit for every slice with a gate of zero
+  static_assert(NTS <= 32, "one bit per slice");
+  const Spot p = take_spot(a, true, &ticket, zeros, CT);
   const int s = a.S - 1 - p.u;
-  const int cg = threadIdx.x % NCG, ts = threadIdx.x / NCG;
-  const int nominal = p.tile * CT + cg * VEC, c0 = group_start<VEC>(nominal, a.C);
-  const int tseg = s * SEG;
-  const int trows = min(SEG, a.T - tseg), rows = trows - ts * L;  // of the segment, from the slice
+  const int tseg = s * SEG, trows = min(SEG, a.T - tseg);
+  const Lane q = lane_of<S>(threadIdx.x, p.tile, a.C, trows);
+  const int cg = q.cg, ts = q.ts, c0 = q.c0;
   const int64_t dense = ((int64_t)p.b * a.T + tseg) * a.C;
-  const uint32_t doff = (uint32_t)(ts * L) * (uint32_t)a.C + c0;
   // the channel that a scanning thread takes (the first CT the gradients, the next CT the states), and
   // what it starts from
   const int k0 = threadIdx.x % CT, group = p.tile * CT + k0 / VEC * VEC;
@@ -344,29 +517,26 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     const auto rf = segment_buffer<T>(a.f, p.b * a.fb + tseg * a.ft, a.ft, trows, a.C);
     const auto rx = segment_buffer<T>(a.x, p.b * a.xb + tseg * a.xt, a.xt, trows, a.C);
     const auto rd = segment_buffer<T>(a.dh, dense, a.C, trows, a.C);
-    load_slice<T, VEC, L>(rf, (uint32_t)(ts * L) * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
-    load_slice<T, VEC, L>(rx, (uint32_t)(ts * L) * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
-    load_slice<T, VEC, L>(rd, doff, (uint32_t)a.C, dh);
+    load_slice<T, VEC, L>(rf, q.t0 * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
+    load_slice<T, VEC, L>(rx, q.t0 * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
+    load_slice<T, VEC, L>(rd, q.t0 * (uint32_t)a.C + c0, (uint32_t)a.C, dh);
     if (real && threadIdx.x < 2 * CT) {
       if (threadIdx.x >= CT)
         from = a.carry[((int64_t)p.b * a.S + s) * a.C + c];
       else if (p.u == 0 && a.state_in)
         from = a.state_in[(int64_t)p.b * a.C + c];
     }
-    slice_gates<T, VEC, L>(f, rows, trows < SEG, v);
+    slice_gates<T, VEC, L>(f, q.rows, trows < SEG, v);
   }
+  {
+    float A[VEC], H[VEC], G[VEC];
+    slice_pairs<COMP, true, T, VEC, L>(v, x, dh, A, H, G, zeros + cg * VEC, ts);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    float A = 1.0f, H = 0.0f, G = 0.0f;
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      A = times_gamma(v[l][i], A);
-      H = advance<COMP>(v[l][i], H, (float)x[l][i]);
-      G = fmaf(A, (float)dh[l][i], G);
+    for (int i = 0; i < VEC; ++i) {
+      sA[ts][cg * VEC + i] = A[i];
+      sH[ts][cg * VEC + i] = H[i];
+      sG[ts][cg * VEC + i] = G[i];
     }
-    sA[ts][cg * VEC + i] = A;
-    sH[ts][cg * VEC + i] = H;
-    sG[ts][cg * VEC + i] = G;
   }
   lds_barrier();
   if (threadIdx.x < CT && real) {
@@ -379,6 +549,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
       G = fmaf(Ak, G, Gk);
       A *= Ak;
     }
+    A = kept(A, zeros[k0] != 0);
     uint64_t* word = a.words + ((int64_t)p.chain * a.S + p.u) * CT + k0;
     const bool last = p.u == a.S - 1;
     float r = from;
@@ -403,36 +574,64 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     }
   }
   lds_barrier();
-  if (nominal >= a.C) return;
-  float d[L][VEC], r[VEC];
+  const Lane o = lane_again<S>(p.tile, a.C, trows);
+  if (o.nominal >= a.C) return;
+  const uint32_t first = o.t0 * (uint32_t)a.C + o.c0;
+  float d[L][VEC], h[VEC];  // h_{t-1} - x, or h_{t-1}
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    float h = sH[ts][cg * VEC + i];
-    r[i] = fmaf(sR[ts][cg * VEC + i], rin[cg * VEC + i], sG[ts][cg * VEC + i]);
+    h[i] = sH[o.ts][o.cg * VEC + i];
 #pragma unroll
     for (int l = 0; l < L; ++l) {
       const float xv = (float)x[l][i];
-      d[l][i] = COMP ? h - xv : h;
-      h = advance<COMP>(v[l][i], h, xv);
+      d[l][i] = COMP ? h[i] - xv : h[i];
+      if (l < L - 1) h[i] = advance<COMP>(v[l][i], sign_of(v[l][i]), h[i], xv);
+    }
+  }
+  if (__builtin_expect(!all_finite(h), 0)) {
+    const Again<VEC, L> g(v);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      h[i] = sH[o.ts][o.cg * VEC + i];
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        const float xv = (float)x[l][i];
+        d[l][i] = COMP ? h[i] - xv : h[i];
+        h[i] = advance_ieee<COMP>(g.v[l][i], h[i], xv);
+      }
     }
   }
   const auto rdx = segment_buffer<T>(a.h, dense, a.C, trows, a.C);
   const auto rdf = segment_buffer<T>(a.df, dense, a.C, trows, a.C);
-#pragma unroll
-  for (int l = L - 1; l >= 0; --l) {
-    float dx[VEC], df[VEC];
+  // runs and stores the slice; whether the gradient that leaves it is finite
+  auto run = [&](auto ieee, const float(&v)[L][VEC]) {
+    constexpr bool IEEE = decltype(ieee)::value;
+    float r[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      const float w = v[l][i], q = (float)dh[l][i] + r[i];
-      r[i] = times_gamma(w, q);
-      dx[i] = COMP ? times_omg(w, q) : q;
-      // gamma (1 - gamma) = s (1 - s) for either sign of f
-      df[i] = fmaf(-w, w, fabsf(w)) * (q * d[l][i]);
+      const int c = o.cg * VEC + i;
+      r[i] = IEEE ? run_end(sR[o.ts][c], rin[c], sG[o.ts][c], (zeros[c] >> o.ts >> 1) != 0)
+                  : fmaf(sR[o.ts][c], rin[c], sG[o.ts][c]);
     }
-    const uint32_t off = (doff + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
-    buffer_store_vec<T, VEC>(rdx, off, dx);
-    buffer_store_vec<T, VEC>(rdf, off, df);
-  }
+#pragma unroll
+    for (int l = L - 1; l >= 0; --l) {
+      float dx[VEC], df[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float w = v[l][i], q = (float)dh[l][i] + r[i];
+        const uint32_t m = sign_of(w);
+        r[i] = IEEE ? times_gamma_ieee(w, q) : times_gamma(w, m, q);
+        dx[i] = !COMP ? q : IEEE ? times_omg_ieee(w, q) : times_omg(w, m, q);
+        // gamma (1 - gamma) = s (1 - s) for either sign of f
+        df[i] = fmaf(-w, w, fabsf(w)) * (q * d[l][i]);
+      }
+      const uint32_t off = (first + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
+      buffer_store_vec<T, VEC>(rdx, off, dx);
+      buffer_store_vec<T, VEC>(rdf, off, df);
+    }
+    return all_finite(r);
+  };
+  if (__builtin_expect(!run(std::false_type(), v), 0)) run(std::true_type(), Again<VEC, L>(v).v);
 }
 
 // No tokens: the gradient passes through
@@ -458,7 +657,7 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a) {
   const vec_t<float, VEC> h0 = load_vec<float, VEC>(st);
   float h[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h[i] = advance<COMP>(gate_of((float)f[i]), h0[i], (float)x[i]);
+  for (int i = 0; i < VEC; ++i) h[i] = advance_ieee<COMP>(gate_of((float)f[i]), h0[i], (float)x[i]);
   if (c == nominal) {
     store_vec<float, VEC>(st, h);
     store_vec<T, VEC>(out, h);
