@@ -43,7 +43,8 @@ class JoinGrads(NamedTuple):
 # ---- checks and parameter blocks, by the tensors' metadata -----------------------------------------
 # A call's checks depend on shapes, strides, dtypes and devices alone. They run on those (a tuple per
 # tensor) and are remembered with the parameter block they led to, so a repeated call costs one
-# look-up: 1 us instead of 3 for the gated norm of one token.
+# look-up: 1 us instead of 3 for the gated norm of one token. Scalars enter as Python numbers: a tensor
+# would be looked up by its identity, whatever it holds by then.
 _SHAPE, _STRIDE, _DTYPE, _DEVICE = range(4)
 
 
@@ -136,7 +137,7 @@ def _on_device(fn):
             out = fn(*args, **kw)
         if inner != outer:
             for t in (*args, *kw.values()):
-                if isinstance(t, torch.Tensor):
+                if isinstance(t, torch.Tensor) and t.is_cuda:  # (a scalar may be a host tensor)
                     t.record_stream(inner)
             for t in out if isinstance(out, tuple) else (out,):
                 if isinstance(t, torch.Tensor):
@@ -216,7 +217,7 @@ def gated_norm(x: torch.Tensor, gate: Optional[torch.Tensor] = None,
     ``gate`` has x's shape (None: no gate), ``weight`` is float32 [D], or [H, D] with weights per
     head (None: ones), ``act`` "silu" or "sigmoid". Also takes ``stream``. Returns a dense tensor of
     x's shape and dtype."""
-    p, _ = _norm_plan(_sig(x), _sig(gate), _sig(weight), None, eps, act)
+    p, _ = _norm_plan(_sig(x), _sig(gate), _sig(weight), None, float(eps), act)
     y = _out(x, out, "out")
     gka._check(gka.load().gka_gated_norm(p, x.data_ptr(), _ptr(gate), _ptr(weight), y.data_ptr(),
                                          _stream(x)))
@@ -229,7 +230,7 @@ def gated_norm_bwd(x: torch.Tensor, gate: Optional[torch.Tensor], weight: Option
                    workspace: Optional[torch.Tensor] = None):
     """gka_gated_norm_bwd: (dx, dgate, dweight) of gated_norm, given dy (dense, x's shape). dgate
     and dweight are None without a gate or weight. Also takes ``stream``."""
-    p, need = _norm_plan(_sig(x), _sig(gate), _sig(weight), _sig(dy), eps, act)
+    p, need = _norm_plan(_sig(x), _sig(gate), _sig(weight), _sig(dy), float(eps), act)
     dx = _new(x)
     dgate = None if gate is None else torch.empty_like(dx)
     dweight = None if weight is None else torch.empty_like(weight)
@@ -280,7 +281,7 @@ def join(res: torch.Tensor, y: torch.Tensor, gate: Optional[torch.Tensor] = None
     ``out`` may be ``res`` itself (dense), which updates the stream in place. Also takes
     ``stream``. Returns (res_out, n); n, in y's dtype, is None without ``w_pre``."""
     p, _ = _join_plan(_sig(res), _sig(y), _sig(gate), _sig(w_post), _sig(scale), _sig(w_pre), None,
-                      None, alpha, eps, act)
+                      None, float(alpha), float(eps), act)
     res_out = _out(res, out, "out")
     n = None if w_pre is None else _out(y, n_out, "n_out")
     gka._check(gka.load().gka_join(
@@ -299,7 +300,7 @@ def join_bwd(res: torch.Tensor, y: torch.Tensor, dres_out: torch.Tensor,
     and the gradients ``dres_out`` (dense, res's shape and dtype) and ``dn`` (dense, y's; exactly
     when ``w_pre`` is given) to its two results. Also takes ``stream``."""
     p, need = _join_plan(_sig(res), _sig(y), _sig(gate), _sig(w_post), _sig(scale), _sig(w_pre),
-                         _sig(dres_out), _sig(dn), alpha, eps, act)
+                         _sig(dres_out), _sig(dn), float(alpha), float(eps), act)
     dres, dy = _new(res), _new(y)
     dgate = None if gate is None else torch.empty_like(dy)
     dws = [None if w is None else torch.empty_like(w) for w in (w_post, scale, w_pre)]
@@ -333,7 +334,7 @@ def _recur_plan(x, f, state, dh, dstate, complement, step):
     if dh is not None:
         _same(x, dh, "dh", True)
     lib = gka.load()
-    p = ctypes.byref(gka.GkaRecurParams(B, T, C, int(bool(complement)), _CODE.get(x[_DTYPE], -1),
+    p = ctypes.byref(gka.GkaRecurParams(B, T, C, int(complement), _CODE.get(x[_DTYPE], -1),
                                         *strides))
     return (p, int(lib.gka_recur_carry_bytes(p)), int(lib.gka_recur_workspace_bytes(p)),
             int(lib.gka_recur_bwd_workspace_bytes(p)))
@@ -349,8 +350,8 @@ def recur(x: torch.Tensor, f: torch.Tensor, state: Optional[torch.Tensor] = None
     ``state`` (optional, float32 [B, C]) is read as the initial state and overwritten with the
     final one. With ``return_carry`` the call returns (h, carry), carry being what ``recur_bwd``
     takes. Also takes ``stream``."""
-    p, carry_bytes, need, _ = _recur_plan(_sig(x), _sig(f), _sig(state), None, None, complement,
-                                          False)
+    p, carry_bytes, need, _ = _recur_plan(_sig(x), _sig(f), _sig(state), None, None,
+                                          bool(complement), False)
     h = _out(x, out, "out")
     carry = x.new_empty(carry_bytes // 4, dtype=torch.float32) if return_carry else None
     ws = _scratch(x, workspace, need)
@@ -364,7 +365,7 @@ def recur_step(x: torch.Tensor, f: torch.Tensor, state: torch.Tensor, complement
                out: Optional[torch.Tensor] = None):
     """gka_recur_step: one token, x and f [B, C]; updates ``state`` (float32 [B, C]) in place and
     returns h [B, C]. Also takes ``stream``."""
-    p = _recur_plan(_sig(x), _sig(f), _sig(state), None, None, complement, True)[0]
+    p = _recur_plan(_sig(x), _sig(f), _sig(state), None, None, bool(complement), True)[0]
     h = _out(x, out, "out")
     gka._check(gka.load().gka_recur_step(p, x.data_ptr(), f.data_ptr(), h.data_ptr(), _ptr(state),
                                          _stream(x)))
@@ -379,7 +380,7 @@ def recur_bwd(x: torch.Tensor, f: torch.Tensor, dh: torch.Tensor, carry: torch.T
     call and ``dstate``, the gradient to the final state (float32 [B, C], None: zero; it is left as
     it is). The returned dstate is the gradient to the initial state. Also takes ``stream``."""
     p, carry_bytes, _, need = _recur_plan(_sig(x), _sig(f), None, _sig(dh), _sig(dstate),
-                                          complement, False)
+                                          bool(complement), False)
     _float32(_sig(x), _sig(carry), (carry_bytes // 4,), "carry")
     dx, df = _new(x), _new(x)
     ds = x.new_empty((x.shape[0], x.shape[2]), dtype=torch.float32)

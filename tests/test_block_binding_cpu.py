@@ -1,0 +1,60 @@
+"""The binding of the block operators without a GPU: what its calls hand to the library, recorded by a
+stand-in for it."""
+import pytest
+import torch
+
+from test_ridge_regression_amd import block, gka
+
+
+class Library:
+    """Records the parameter block of every call; sizes are 0."""
+
+    def __init__(self):
+        self.last = None
+
+    def __getattr__(self, name):
+        def call(p, *args):
+            if not name.endswith("_bytes"):
+                self.last = p._obj
+            return 0
+        return call
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(gka, "load", lambda: lib)
+    monkeypatch.setattr(block, "_stream", lambda x: 0)
+    return lib
+
+
+def on_cpu(fn):
+    """The call without the wrapper that refuses host tensors."""
+    return fn.__wrapped__
+
+
+X = torch.zeros(4, 2, 16)
+W = torch.ones(16)
+F = torch.zeros(2, 5, 8)
+SCALAR_CALLS = {
+    "gated_norm eps": (lambda v: on_cpu(block.gated_norm)(X, eps=v), "eps"),
+    "gated_norm_bwd eps": (lambda v: on_cpu(block.gated_norm_bwd)(X, None, None, X, eps=v), "eps"),
+    "join eps": (lambda v: on_cpu(block.join)(X, X, eps=v), "eps"),
+    "join alpha": (lambda v: on_cpu(block.join)(X, X, alpha=v), "alpha"),
+    "join_bwd alpha": (lambda v: on_cpu(block.join_bwd)(X, X, X, alpha=v), "alpha"),
+    "recur complement": (lambda v: on_cpu(block.recur)(F, F, complement=v), "complement"),
+    "recur_step complement": (lambda v: on_cpu(block.recur_step)(F[:, 0], F[:, 0], torch.zeros(2, 8),
+                                                                 complement=v), "complement"),
+}
+
+
+@pytest.mark.parametrize("name", SCALAR_CALLS)
+def test_a_scalar_tensor_is_read_by_every_call(lib, name):
+    """A learnt residual scale, say: the same tensor holds another value at the next call."""
+    call, field = SCALAR_CALLS[name]
+    value = torch.tensor(1.0)
+    call(value)
+    assert getattr(lib.last, field) == 1
+    value.fill_(0.0 if field == "complement" else 0.25)
+    call(value)
+    assert getattr(lib.last, field) == value.item()

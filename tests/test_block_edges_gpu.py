@@ -129,3 +129,20 @@ def test_recur_of_the_largest_values(T, dtype):
     st = on_gpu(state, "fp32")
     h = block.recur_step(on_gpu(x[:, 0], dtype), on_gpu(f[:, 0], dtype), st)
     same({"h": h[:, None]}, {"h": tuple(v[:, :1] for v in want["h"])})
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda"])
+@pytest.mark.parametrize("side", [False, True])
+def test_a_scalar_tensor_is_read_by_every_call(device, side):
+    """A residual scale that is learnt: the same tensor with another value gives the other result."""
+    rng = np.random.default_rng(11)
+    res, y, g = (on_gpu(rng.standard_normal((5, 64)), "fp32") for _ in range(3))
+    torch.cuda.synchronize()
+    kw = {"stream": torch.cuda.Stream()} if side else {}
+    alpha = torch.tensor(0.5, device=device)
+    for value in (0.5, 0.125):
+        alpha.fill_(value)
+        torch.cuda.synchronize()
+        out, dy = block.join(res, y, alpha=alpha, **kw)[0], block.join_bwd(res, y, g, alpha=alpha, **kw).dy
+        torch.cuda.synchronize()
+        assert torch.equal(out, torch.add(res, y, alpha=value)) and torch.equal(dy, value * g)
