@@ -671,12 +671,14 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a) {
   }
 }
 
-int recur_carry_segments(int T) { return (T + kCarry - 1) / kCarry; }
+// T / per, rounded up without passing T
+static int segments(int T, int per) { return T / per + (T % per != 0); }
+int recur_carry_segments(int T) { return segments(T, kCarry); }
 
 template <typename S>
 static RecurPlan plan_of(int B, int T, int C) {
   RecurPlan pl;
-  pl.S = (T + S::SEG - 1) / S::SEG;
+  pl.S = segments(T, S::SEG);
   pl.tiles = (C + S::CT - 1) / S::CT;
   const size_t chains = (size_t)B * pl.tiles;
   // words that a look-back from a chain's start may read, the words, then one counter per chain

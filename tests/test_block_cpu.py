@@ -230,3 +230,14 @@ def test_host_code_under_asan_and_ubsan(tmp_path):
                        text=True)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
     assert "passed" in r.stdout and "failed" not in r.stdout
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T", [(1 << 31) - 1, (1 << 31) - 100, (1 << 31) - 255, (1 << 31) - 256, 1 << 30])
+def test_recur_refuses_more_segments_than_a_grid(lib, T, dtype):
+    """Sequences near the largest 32-bit length: the count of segments rounds up past 32 bits."""
+    p = recur(B=1, T=T, C=1, dtype=dtype, xb=T, xt=1, fb=T, ft=1)
+    assert lib.gka_recur(p, V[0], V[1], V[2], V[3], None, V[5], 1 << 39, None) == 2
+    assert lib.gka_recur_bwd(p, V[0], V[1], V[2], V[3], None, V[5], V[6], V[7], V[8], 1 << 39, None) == 2
+    assert lib.gka_recur_workspace_bytes(p) == lib.gka_recur_bwd_workspace_bytes(p) == 0
+    assert lib.gka_recur_carry_bytes(p) == 0
