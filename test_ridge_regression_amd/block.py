@@ -319,6 +319,8 @@ def _recur_plan(x, f, state, dh, dstate, complement, step):
     shape = x[_SHAPE]
     if len(shape) != (2 if step else 3):
         raise ValueError("x must be [B, C]" if step else "x must be [B, T, C]")
+    if max(shape) > 0x7fffffff:  # the parameter block would hold it modulo 2^32
+        raise ValueError(f"x of shape {tuple(shape)}: its dimensions must be below 2^31")
     _same(x, f, "f", False)
     B, C = shape[0], shape[-1]
     T = 1 if step else shape[1]

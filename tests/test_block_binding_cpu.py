@@ -58,3 +58,27 @@ def test_a_scalar_tensor_is_read_by_every_call(lib, name):
     value.fill_(0.0 if field == "complement" else 0.25)
     call(value)
     assert getattr(lib.last, field) == value.item()
+
+
+@pytest.mark.parametrize("shape", [((1 << 32) + 3, 1, 1), (1, (1 << 32) + 5, 1), (1, 1, (1 << 32) + 8)])
+def test_recur_refuses_sizes_beyond_32_bits(lib, shape):
+    """A dimension that the parameter block would hold modulo 2^32: the call would cover a part of it."""
+    x = torch.empty(shape, device="meta")
+    with pytest.raises(ValueError):
+        on_cpu(block.recur)(x, x)
+    carry = torch.empty(0, device="meta", dtype=torch.float32)
+    with pytest.raises(ValueError):
+        on_cpu(block.recur_bwd)(x, x, x, carry)
+    if shape[1] == 1:
+        row, state = x[:, 0], torch.empty(shape[0], shape[2], device="meta")
+        with pytest.raises(ValueError):
+            on_cpu(block.recur_step)(row, row, state)
+
+
+def test_norm_and_join_hand_wide_rows_over_whole(lib):
+    """Their rows may be as wide as the C side checks: a width beyond 32 bits shows in the stride."""
+    x = torch.empty((1, 1, (1 << 32) + 64), device="meta")
+    on_cpu(block.gated_norm)(x)
+    assert lib.last.x_stride == (1 << 32) + 64
+    on_cpu(block.join)(x, x)
+    assert lib.last.res_stride == lib.last.y_stride == (1 << 32) + 64
