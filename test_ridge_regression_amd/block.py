@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 from typing import NamedTuple, Optional
 
@@ -121,9 +122,13 @@ def _on_device(fn):
     stream of it. On another stream than the caller's current one, what the call allocates comes
     from that stream's pool, and inputs and outputs are marked as used on both streams, so that the
     allocator hands none of their memory out while either still uses it."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        x = args[0] if args else next(iter(kw.values()), None)
+        if not args and first not in kw:
+            return fn(**kw)  # raises the TypeError that names it
+        x = args[0] if args else kw[first]
         device = x.get_device() if isinstance(x, torch.Tensor) else -1
         if device < 0:
             raise ValueError("libgka takes GPU (device) tensors")

@@ -82,3 +82,42 @@ def test_norm_and_join_hand_wide_rows_over_whole(lib):
     assert lib.last.x_stride == (1 << 32) + 64
     on_cpu(block.join)(x, x)
     assert lib.last.res_stride == lib.last.y_stride == (1 << 32) + 64
+
+
+def _first_tensor(monkeypatch, fn, **kw):
+    """What the wrapper of ``fn`` takes for the tensor that names the device, called with keywords."""
+    seen = []
+
+    class Device(torch.Tensor):
+        def get_device(self):
+            seen.append(self.tag)
+            return -1
+    tensors = {}
+    for k, v in kw.items():
+        if isinstance(v, torch.Tensor):
+            v = v.as_subclass(Device)
+            v.tag = k
+        tensors[k] = v
+    with pytest.raises(ValueError):
+        fn(**tensors)
+    return seen[0] if seen else None
+
+
+@pytest.mark.parametrize("fn,first,kw", [
+    (block.gated_norm, "x", {"eps": 1e-5, "x": X}), (block.gated_norm, "x", {"gate": None, "x": X}),
+    (block.gated_norm, "x", {"act": "silu", "gate": X.clone(), "x": X}),
+    (block.gated_norm_bwd, "x", {"dy": X.clone(), "weight": None, "gate": None, "x": X}),
+    (block.join, "res", {"alpha": 0.5, "y": X.clone(), "res": X}),
+    (block.join_bwd, "res", {"dn": None, "dres_out": X.clone(), "y": X.clone(), "res": X}),
+    (block.recur, "x", {"complement": False, "f": F.clone(), "x": F}),
+    (block.recur_step, "x", {"state": torch.zeros(2, 8), "f": F[:, 0], "x": F[:, 0]}),
+    (block.recur_bwd, "x", {"dstate": None, "carry": W, "dh": F, "f": F, "x": F})])
+def test_keywords_in_any_order(monkeypatch, fn, first, kw):
+    assert _first_tensor(monkeypatch, fn, **kw) == first
+
+
+def test_a_missing_tensor_is_named():
+    with pytest.raises(TypeError, match="'x'"):
+        block.gated_norm(gate=X)
+    with pytest.raises(TypeError, match="'res'"):
+        block.join(y=X)

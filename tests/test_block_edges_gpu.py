@@ -146,3 +146,12 @@ def test_a_scalar_tensor_is_read_by_every_call(device, side):
         out, dy = block.join(res, y, alpha=alpha, **kw)[0], block.join_bwd(res, y, g, alpha=alpha, **kw).dy
         torch.cuda.synchronize()
         assert torch.equal(out, torch.add(res, y, alpha=value)) and torch.equal(dy, value * g)
+
+
+def test_keywords_in_any_order():
+    rng = np.random.default_rng(12)
+    x, g = (on_gpu(rng.standard_normal((5, 2, 32)), "bf16") for _ in range(2))
+    assert torch.equal(block.gated_norm(eps=1e-5, gate=g, x=x), block.gated_norm(x, g, eps=1e-5))
+    assert torch.equal(block.gated_norm(gate=None, x=x), block.gated_norm(x))
+    assert torch.equal(block.join(alpha=0.5, y=g, res=x)[0], block.join(x, g, alpha=0.5)[0])
+    assert torch.equal(block.recur(complement=False, f=g, x=x), block.recur(x, g, complement=False))
