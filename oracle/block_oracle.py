@@ -13,6 +13,20 @@ U = 2.0 ** -24
 # gate's exponential, whose argument is rounded (an error of |g| units) and which the sigmoid and
 # its slope use a few times
 PATH = 32
+# Additions that one term of a sum goes through, where fewer than all of them: a sum over a row is up to 16
+# elements of a lane, 6 levels of lanes and 4 of waves (26); a weight gradient is a lane's own rows (10
+# in the longest tests), up to 256 teams of a workgroup, and a column's partial rows: 64 threads of up to
+# 2048 / 64 rows each and 6 levels (304).
+ROW_SUM = 32
+COLUMN_SUM = 304
+
+
+def _row(n):
+    return min(n, ROW_SUM) * U
+
+
+def _column(n):
+    return min(n, COLUMN_SUM) * U
 
 
 def _sigmoid(g):
@@ -42,7 +56,7 @@ def gated_norm_ref(x, gate, weight, eps, act, dy=None):
     a, slope, slope_abs = act_ref(gate, act) if gate is not None else (1.0, 0.0, 0.0)
     k = _units(gate)
     y = xh * w * a
-    sums = D * U  # the mean of x^2, all terms of one sign
+    sums = _row(D)  # the mean of x^2, all terms of one sign
     out = {"y": (y, np.abs(y) * (k * U + sums))}
     if dy is None:
         return out
@@ -58,7 +72,7 @@ def gated_norm_ref(x, gate, weight, eps, act, dy=None):
         axes = (0,) if weight.ndim == 2 else (0, 1)
         t = dy * xh * a
         out["dweight"] = (t.sum(axes), (np.abs(t) * (k * U + sums)).sum(axes)
-                          + np.abs(t).sum(axes) * U * rows * (1 if weight.ndim == 2 else H))
+                          + np.abs(t).sum(axes) * _column(rows * (1 if weight.ndim == 2 else H)))
     return out
 
 
@@ -67,7 +81,7 @@ def join_ref(res, y, gate, w_post, scale, w_pre, alpha, eps, act, dres_out=None,
     rows, C = y.shape
     k = _units(gate)
     k = float(np.max(k)) if np.size(k) else PATH
-    sums = C * U
+    sums = _row(C)
     one = np.ones(C)
     a, slope, slope_abs = act_ref(gate, act) if gate is not None else (1.0, None, None)
     ry = 1.0 / np.sqrt((y * y).mean(-1, keepdims=True) + eps) if w_post is not None else 1.0
@@ -114,15 +128,15 @@ def join_ref(res, y, gate, w_post, scale, w_pre, alpha, eps, act, dres_out=None,
         out["dy"] = (ry * (e - yh * c1),
                      ry * (e_e + np.abs(yh) * e_c1 + (np.abs(e) + np.abs(yh) * c1_abs) * kk))
         t = du * a * yh
-        out["dw_post"] = (t.sum(0), (np.abs(a * yh) * e_du + np.abs(t) * (kk + rows * U)).sum(0))
+        out["dw_post"] = (t.sum(0), (np.abs(a * yh) * e_du + np.abs(t) * (kk + _column(rows))).sum(0))
     else:
         out["dy"] = (e, e_e)
     if scale is not None:
         t = alpha * G * u
-        out["dscale"] = (t.sum(0), (np.abs(alpha * u) * e_G + np.abs(t) * (kk + rows * U)).sum(0))
+        out["dscale"] = (t.sum(0), (np.abs(alpha * u) * e_G + np.abs(t) * (kk + _column(rows))).sum(0))
     if w_pre is not None:
         t = dn * rh
-        out["dw_pre"] = (t.sum(0), (np.abs(dn) * rh_err + np.abs(t) * (kk + rows * U)).sum(0))
+        out["dw_pre"] = (t.sum(0), (np.abs(dn) * rh_err + np.abs(t) * (kk + _column(rows))).sum(0))
     return out
 
 
