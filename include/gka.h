@@ -418,7 +418,8 @@ gka_status gka_join_bwd(const gka_join_params* p, const void* res, const void* y
  *   h_t = gamma_t h_{t-1} + beta_t x_t,  gamma_t = sigmoid(f_t),
  *   beta_t = 1 - gamma_t (complement = 1) or 1 (complement = 0).
  * The gate is given by its logit: near gamma = 1 a 16-bit gamma could not hold how long the
- * memory is, while the logit keeps 1 - gamma to its relative precision. f = +inf keeps the state
+ * memory is, while the logit does; the smaller of gamma and 1 - gamma is computed to
+ * (6 + 1.25 |f|) 2^-24 of itself. f = +inf keeps the state
  * (with complement = 1 the token writes nothing: padding), f = -inf drops it (the first token of
  * a document in a packed row; a state that is not finite leaves NaN, as 0 times infinity does).
  *   B, T, C      batch rows, tokens, channels: B >= 1, T >= 0, C >= 1, B C <= 2^30

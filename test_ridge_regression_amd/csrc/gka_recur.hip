@@ -18,8 +18,8 @@
 // counter in the order in which workgroups start, so whatever a workgroup waits for belongs to one
 // that is running already, and segment 0 waits for nothing.
 //
-// Gates: s = exp(-|f|) / (1 + exp(-|f|)) is the smaller of gamma and 1 - gamma, to its relative
-// precision; a thread keeps v = copysign(s, f) and takes the larger one as 1 - s, rounded to nearest
+// Gates: s = exp(-|f|) / (1 + exp(-|f|)) is the smaller of gamma and 1 - gamma, to (6 + 1.25 |f|) 2^-24 of
+// itself; a thread keeps v = copysign(s, f) and takes the larger one as 1 - s, rounded to nearest
 // (a bias in gamma near 1 would grow with the memory's length).
 //
 // Infinities go as gamma h + beta x takes them. The forms above turn an infinity into NaN at the next step

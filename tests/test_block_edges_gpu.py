@@ -155,3 +155,15 @@ def test_keywords_in_any_order():
     assert torch.equal(block.gated_norm(gate=None, x=x), block.gated_norm(x))
     assert torch.equal(block.join(alpha=0.5, y=g, res=x)[0], block.join(x, g, alpha=0.5)[0])
     assert torch.equal(block.recur(complement=False, f=g, x=x), block.recur(x, g, complement=False))
+
+
+def test_precision_of_the_smaller_sigmoid():
+    """A step from state 1 with x = 0 under f < 0 leaves sigmoid(f) itself: exp2 and the reciprocal to 1 ulp
+    (2 units of 2^-24 each), a sum and a product, and the argument of exp2 rounded twice (1.25 |f| units)."""
+    f = -torch.linspace(0.0, 80.0, 1 << 16, device="cuda")[None]
+    state = torch.ones_like(f)
+    block.recur_step(torch.zeros_like(f), f, state)
+    f, got = num(f), num(state)
+    want = np.exp(f) / (1.0 + np.exp(f))
+    units = np.abs(got / want - 1.0) / 2.0 ** -24
+    assert (units <= 6 + 1.25 * np.abs(f)).all(), units.max()
