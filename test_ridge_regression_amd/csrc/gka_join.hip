@@ -10,10 +10,13 @@
 // which is three dependent sums per row. Weight gradients are summed as in the gated norm: per lane
 // over the team's tokens, the workgroup's teams in LDS, the workgroups by column_sums_kernel.
 //
-// Measured: 16384 bf16 tokens of 4096 channels 122 us forward (5.5 TB/s) and 212 us backward (5.1 TB/s;
-// the card copies 5.1); with a float32 stream, 32768 tokens of 1024 channels 84 us (5.5 TB/s) and 141 us
-// (5.2 TB/s). Slower: the bf16 backward beyond 4096 channels (8192: 3.6 to 4.4 TB/s, one workgroup per
-// CU and nothing loaded ahead) and odd bf16 widths that leave lanes or waves idle (333: 3.6 TB/s).
+// Measured, calls one after another: 16384 bf16 tokens of 4096 channels 122 us forward (5.5 TB/s) and
+// 213 us backward (5.0 TB/s; the card copies 5.1), 7 of which are the weight gradients' second kernel;
+// with a float32 stream, 32768 tokens of 1024 channels 84 us (5.6 TB/s) and 154 us (4.8 TB/s). Slower: the
+// bf16 backward beyond 4096 channels (8192: 3.6 TB/s, 4.3 with a float32 stream; 5120: 3.4; 4099: 2.6),
+// where one workgroup per CU has nothing loaded ahead, the narrower widths as many waves as they need and
+// not what the CU could hold; and odd bf16 widths that leave lanes or waves idle (333: 4.3 TB/s forward,
+// 3.5 backward).
 #include "gka_block.hpp"
 #include "gka_rows.hpp"
 
@@ -125,9 +128,10 @@ struct JoinBwdRow {
 };
 
 // What the compiler derives from a row after this it derives again, instead of holding conversions and
-// gates in registers across the sums. Two vectors per lane then fit 128 registers: 4096 rows of 8192
-// channels, bf16 with a float32 stream, take 171 us (270 with 46 spilled registers). (Loads of the next
-// row during a row, which one vector per lane has, spill again and cost 25 to 50 % here.)
+// gates in registers across the sums. Two vectors per lane then fit 128 registers but for 2 with a float32
+// stream and 6 in float32: 4096 rows of 8192 channels, bf16 with a float32 stream, take 170 us (270 with
+// 46 spilled registers). (Loads of the next row during a row, which one vector per lane has, spill again
+// and cost 25 to 50 % here.)
 template <typename V, int NV>
 __device__ inline void renew(V (&v)[NV]) {
 #pragma unroll

@@ -27,11 +27,12 @@
 // so in them. A slice whose end is not finite is therefore run again, each step that is not finite in the
 // definition's form; finite channels keep their bits. A product of gates that underflows is kept above
 // zero, since an infinite state survives it, while a gate of zero times infinity is NaN. The checks cost a
-// finite call up to 1 % forward and 1 to 2 % backward (4 sequences of 8192 steps by 2048 channels: 133 us
-// without, 136 with them).
+// finite call nothing to 2 % (a forward of one or two rounds of workgroups up to 3 %: 8 sequences of 2048
+// steps by 1024 channels, slices of wider rows, 23.6 us with them and 22.9 without).
 //
-// Measured (bf16): 4 sequences of 8192 steps by 2048 channels 90 us forward (4.5 TB/s) and 133 us
-// backward (5.0 TB/s); one of 131072 steps by 1024 channels 180 us (4.5 TB/s) and 315 us (4.3 TB/s).
+// Measured (bf16): 4 sequences of 8192 steps by 2048 channels 90 us forward (4.5 TB/s) and 134 us
+// backward (5.0 TB/s); one of 131072 steps by 1024 channels 180 us (4.5 TB/s) and 316 us (4.3 TB/s).
+// float32: 149 us (5.4 TB/s) and 246 us (5.5 TB/s), 306 us (5.3 TB/s) and 535 us (5.0 TB/s).
 // The card copies 5.1 TB/s; what is between is the start of a workgroup (counter, loads, scan,
 // look-back), which only the other workgroups' loads cover: the same kernel without the look-back
 // (one segment per chain) reaches 5.0 to 5.5 TB/s.
@@ -57,21 +58,30 @@ struct Shape {
 constexpr int kCarry = 128;  // steps between the carry's rows: every backward's segment
 
 // Which shape a call takes. Two channels per thread fill the card with 8 waves per SIMD; in float32
-// that is 8 bytes per thread and row and reaches 5.0 to 5.3 TB/s. bf16 rows of 8 bytes are 4 channels,
-// at the price of 128 registers and 4 waves:
-// - Forward: 4 channels. With 2, one sequence of 131072 steps by 1024 channels takes 205 us, with 4 184.
-//   A chain's end states pass from segment to segment at about 0.1 us each, so a long sequence wants
-//   few, long segments (233 us with the short shape). The short shape has two workgroups per CU, so
-//   that one loads while the other scans or waits, and half-empty segments are rarer: 40 us for 256
-//   sequences of 128 steps, 50 for 64 of 512 (1024 channels), where the long one takes 68 and 58. They
-//   meet between 4096 and 8192 steps (4 sequences of 2048 channels: 52 us short and 55 long at 4096, 90
-//   and 95 at 8192; one of 4096 channels at 8192: 53 and 51). Up to 2^24 elements in sequences of more
-//   than 1024 steps, a round or two of workgroups in all, more waves with half the work each are worth
-//   more: with 2 channels 15.6 us instead of 16.8 for 4 x 2048 x 1024, 24.0 instead of 25.9 for
-//   2 x 4096 x 2048 (but 23.4 instead of 22.3 for 8 x 1024 x 2048, 50 instead of 46 for 16 x 2048 x 1024).
-// - Backward: 2 channels (4 x 8192 x 2048: 139 us, 150 with 4; 8 x 2048 x 1024: 38.6 and 41.8), unless the
-//   sequence is long and there are too few tiles of 64 channels to fill the card: at 131072 steps 1024
-//   channels take 323 us with 4 and 354 with 2, 2048 in all 624 to 644 and 640 to 653, 4096 1190 and 1123.
+// that is 8 bytes per thread and row and reaches 5.0 to 5.4 TB/s. bf16 rows of 8 bytes are 4 channels,
+// at the price of 128 registers and 4 waves. Microseconds a call (side by side on one card; cards differ
+// by up to 5 %), batch x steps x channels, for
+// [2 channels in segments of 256 | 4 in segments of 128 | 4 in segments of 256]:
+// - Forward beyond 4096 steps, the third: a chain's end states pass from segment to segment at about
+//   0.1 us each, so a long sequence wants few, long segments: 1 x 131072 x 1024 [210 | 231 | 184],
+//   1 x 32768 x 4096 [188 | 185 | 173]. With more tiles than CUs the second would still be ahead by 2 to
+//   9 % (4 x 4352 x 2048 [56 | 53 | 58], 8 x 8192 x 2048 [191 | 164 | 169]), with few the first at first
+//   (2 x 4352 x 1024 [20 | 23 | 23], 2 x 8192 x 1024 [29 | 33 | 30], 2 x 16384 x 1024 [55 | 58 | 52]).
+// - Forward up to there, the second: it has two workgroups per CU, so that one loads while the other
+//   scans or waits, and half-empty segments are rarer: 256 x 128 x 1024 [56 | 40 | 67],
+//   64 x 512 x 1024 [51 | 52 | 55], 16 x 2048 x 1024 [53 | 50 | 52], 8 x 4096 x 2048 [104 | 92 | 98];
+// - but the first for up to 2^24 elements in more than 1024 steps, a round or two of workgroups in all,
+//   where more waves with half the work each are worth more: 2 x 4096 x 1024 [17.0 | 20.5 | 17.7],
+//   8 x 1280 x 1024 [18.6 | 19.6 | 21.2], 4 x 1536 x 2048 [20.0 | 21.1 | 22.7]. They meet between 2^24 and
+//   2^25 (4 x 2048 x 2048 [27.1 | 27.8 | 28.9], 6 x 4096 x 1024 [41.8 | 42.2 | 41.0], 12 x 2048 x 1024
+//   [40.6 | 39.3 | 40.3]); at 1024 steps between 2^23 and 2^24 (8 x 1024 x 1024 [15.4 | 16.1 | 15.9],
+//   8 x 1024 x 2048 [27.3 | 26.3 | 26.4]).
+// - Backward [2 | 4 channels, segments of 128]: 2 (4 x 8192 x 2048 [139 | 149], 8 x 2048 x 1024
+//   [42.8 | 47.0], 4 x 4096 x 1024 [43.7 | 46.9], 2 x 4096 x 1024 [24.5 | 25.9]), unless the sequence is
+//   long and there are too few tiles of 64 channels to fill the card: 1 x 6144 x 1024 [23.9 | 23.4],
+//   1 x 8192 x 512 [20.9 | 19.9], 1 x 131072 x 1024 [341 | 312], 1 x 131072 x 512 [204 | 162]. 2048 channels
+//   in all are even from 6144 steps on (2 x 8192 x 1024 [49.0 | 47.0], 2 x 131072 x 1024 [629 | 627]), 4096
+//   are not (4 x 8192 x 1024 [77 | 84]).
 template <typename Fn>
 inline auto with_forward(int dtype, int B, int T, int C, Fn fn) {
   if (dtype != 0) return fn(Shape<float, 2, 64, 256, 1024, 8>{});
@@ -292,8 +302,8 @@ __device__ inline void publish_state(uint64_t* word, float h) { publish(word, 1u
 // state is the same chain of fused multiply-adds whichever state it was taken from, so results do
 // not depend on timing. The words before a chain's first are another chain's (or the padding of the
 // workspace): position 0 only ever holds a state, which overrides whatever came before it.
-// A window of 16 words shortens the chain of one narrow sequence (a million steps of 16 channels: 242 us,
-// 328 with 8) but its registers cost every other case 3 to 7 %.
+// A window of 16 words shortens the chain of one narrow sequence (a million steps of 16 channels: 238 us
+// forward and 385 backward, 318 and 622 with 8) but its registers cost every other case 3 to 15 %.
 constexpr int kLook = 8;
 template <int CT>
 __device__ inline float look_back(const uint64_t* at) {
@@ -319,20 +329,17 @@ __device__ inline float look_back(const uint64_t* at) {
 // The workgroup's chain (batch row and tile) and its position in it, from the chain's counter.
 // Workgroups go round the 8 XCDs, and so do neighbouring tiles. `near`: where every chain has one XCD
 // (their number is a multiple of 8), neighbours go to the same one. Tiles of rows that are no whole
-// cache lines share lines, which one L2 then reads and writes once: 16 sequences of 2048 steps by 1000
-// channels take 49 us forward and 78 us backward, 55 and 91 without; 8 of 8192 by 1001 105 and 171,
-// 127 and 210 (the backward with 4 channels per thread). With whole lines the forward is better off dealt round (8 of 1024 by 2048: 22.1 us,
-// 24.4 with `near`), the backward is not (4 of 8192 by 2048: 151 us, 147 with `near`).
+// cache lines share lines, which one L2 then reads and writes once: without `near` 16 sequences of 2048
+// steps by 1000 channels take 16 % more forward and 28 % more backward, 8 of 8192 by 1001 22 % and 35 %.
+// With whole lines the forward is as well off dealt round (8 of 1024 by 2048 take 3 % more with `near`, 4
+// of 8192 by 2048 and one of 131072 by 1024 the same), the backward is not (4 of 8192 by 2048: 14 % more
+// without).
 struct Spot {
   int chain, b, tile, u;
 };
 __device__ inline Spot take_spot(const RecurArgs& a, bool near, int* lds, uint32_t* zeros,
                                  int channels) {
   Spot p;
-  // Every argument is read at the start, in one round trip, not in a second one after the counter's: 8
-  // sequences of 2048 steps by 1024 channels 23.5 us forward, 25.1 without.
-  asm volatile("" ::"s"(a.x), "s"(a.f), "s"(a.h), "s"(a.state_in), "s"(a.carry), "s"(a.words), "s"(a.xb),
-               "s"(a.xt), "s"(a.fb), "s"(a.ft), "s"(a.T), "s"(a.C));
   const int chains = a.B * a.tiles;
   const int q = blockIdx.x % chains;
   p.chain = near && chains % 8 == 0 ? q % 8 * (chains / 8) + q / 8 : q;
@@ -399,6 +406,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
   lds_barrier();
   if (threadIdx.x < CT && group < a.C) {
     // the slices' exclusive pairs, in place, and the segment's pair (At, Ht)
+    const uint32_t zero = zeros[threadIdx.x];
     float At = 1.0f, Ht = 0.0f;
 #pragma unroll 16
     for (int k = 0; k < NTS; ++k) {
@@ -408,7 +416,6 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
       Ht = fmaf(Ak, Ht, Hk);
       At *= Ak;
     }
-    const uint32_t zero = zeros[threadIdx.x];
     At = kept(At, zero != 0);
     uint64_t* word = a.words + ((int64_t)p.chain * a.S + p.u) * CT + threadIdx.x;
     const bool last = p.u == a.S - 1;
@@ -540,6 +547,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
   }
   lds_barrier();
   if (threadIdx.x < CT && real) {
+    const uint32_t zero = zeros[k0];
     float A = 1.0f, G = 0.0f;
 #pragma unroll 16
     for (int k = NTS - 1; k >= 0; --k) {
@@ -549,7 +557,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
       G = fmaf(Ak, G, Gk);
       A *= Ak;
     }
-    A = kept(A, zeros[k0] != 0);
+    A = kept(A, zero != 0);
     uint64_t* word = a.words + ((int64_t)p.chain * a.S + p.u) * CT + k0;
     const bool last = p.u == a.S - 1;
     float r = from;
@@ -574,13 +582,12 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     }
   }
   lds_barrier();
-  const Lane o = lane_again<S>(p.tile, a.C, trows);
-  if (o.nominal >= a.C) return;
-  const uint32_t first = o.t0 * (uint32_t)a.C + o.c0;
+  if (q.nominal >= a.C) return;
+  const uint32_t first = q.t0 * (uint32_t)a.C + c0;
   float d[L][VEC], h[VEC];  // h_{t-1} - x, or h_{t-1}
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    h[i] = sH[o.ts][o.cg * VEC + i];
+    h[i] = sH[ts][cg * VEC + i];
 #pragma unroll
     for (int l = 0; l < L; ++l) {
       const float xv = (float)x[l][i];
@@ -592,7 +599,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     const Again<VEC, L> g(v);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      h[i] = sH[o.ts][o.cg * VEC + i];
+      h[i] = sH[ts][cg * VEC + i];
 #pragma unroll
       for (int l = 0; l < L; ++l) {
         const float xv = (float)x[l][i];
@@ -609,21 +616,21 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     float r[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      const int c = o.cg * VEC + i;
-      r[i] = IEEE ? run_end(sR[o.ts][c], rin[c], sG[o.ts][c], (zeros[c] >> o.ts >> 1) != 0)
-                  : fmaf(sR[o.ts][c], rin[c], sG[o.ts][c]);
+      const int c = cg * VEC + i;
+      r[i] = IEEE ? run_end(sR[ts][c], rin[c], sG[ts][c], (zeros[c] >> ts >> 1) != 0)
+                  : fmaf(sR[ts][c], rin[c], sG[ts][c]);
     }
 #pragma unroll
     for (int l = L - 1; l >= 0; --l) {
       float dx[VEC], df[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float w = v[l][i], q = (float)dh[l][i] + r[i];
+        const float w = v[l][i], g = (float)dh[l][i] + r[i];
         const uint32_t m = sign_of(w);
-        r[i] = IEEE ? times_gamma_ieee(w, q) : times_gamma(w, m, q);
-        dx[i] = !COMP ? q : IEEE ? times_omg_ieee(w, q) : times_omg(w, m, q);
+        r[i] = IEEE ? times_gamma_ieee(w, g) : times_gamma(w, m, g);
+        dx[i] = !COMP ? g : IEEE ? times_omg_ieee(w, g) : times_omg(w, m, g);
         // gamma (1 - gamma) = s (1 - s) for either sign of f
-        df[i] = fmaf(-w, w, fabsf(w)) * (q * d[l][i]);
+        df[i] = fmaf(-w, w, fabsf(w)) * (g * d[l][i]);
       }
       const uint32_t off = (first + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
       buffer_store_vec<T, VEC>(rdx, off, dx);
@@ -642,7 +649,7 @@ __global__ __launch_bounds__(256) void recur_pass_kernel(const float* in, float*
 
 // One token: VEC channels per thread, the row's last group as in the scans (each channel is stored by
 // its owner alone: the state is updated in place). 8192 sequences of 4096 channels in bf16 81 us (5.8
-// TB/s); 256 of 1024 2.7 us, where any kernel takes 2.
+// TB/s); 256 of 1024 3.0 us, where any kernel takes 2.
 template <typename T, int VEC, bool COMP>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a) {
   const int per = (a.C + VEC - 1) / VEC;
@@ -657,7 +664,14 @@ __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a) {
   const vec_t<float, VEC> h0 = load_vec<float, VEC>(st);
   float h[VEC];
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) h[i] = advance_ieee<COMP>(gate_of((float)f[i]), h0[i], (float)x[i]);
+  for (int i = 0; i < VEC; ++i) {
+    const float v = gate_of((float)f[i]);
+    h[i] = advance<COMP>(v, sign_of(v), h0[i], (float)x[i]);
+  }
+  if (__builtin_expect(!all_finite(h), 0)) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) h[i] = advance_ieee<COMP>(gate_of((float)f[i]), h0[i], (float)x[i]);
+  }
   if (c == nominal) {
     store_vec<float, VEC>(st, h);
     store_vec<T, VEC>(out, h);
