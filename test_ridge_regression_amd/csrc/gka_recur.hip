@@ -27,8 +27,8 @@
 // so in them. A slice whose end is not finite is therefore run again, each step that is not finite in the
 // definition's form; finite channels keep their bits. A product of gates that underflows is kept above
 // zero, since an infinite state survives it, while a gate of zero times infinity is NaN. The checks cost a
-// finite call nothing to 2 % (a forward of one or two rounds of workgroups up to 3 %: 8 sequences of 2048
-// steps by 1024 channels, slices of wider rows, 23.6 us with them and 22.9 without).
+// finite call nothing to 2 % (8 sequences of 2048 steps by 1024 channels, slices of wider rows: 23.4 us
+// with them and 22.9 without).
 //
 // Measured (bf16): 4 sequences of 8192 steps by 2048 channels 90 us forward (4.5 TB/s) and 134 us
 // backward (5.0 TB/s); one of 131072 steps by 1024 channels 180 us (4.5 TB/s) and 316 us (4.3 TB/s).
@@ -197,7 +197,8 @@ __device__ inline void slice_gates(const vec_t<T, VEC> (&f)[L], int rows, bool t
 
 // Where a thread's vectors lie: VEC channels from c0 on (its own from `nominal` on) of L steps from step t0
 // of the segment on, of which `rows` steps are left before the segment's end. lane_again derives it a second
-// time, so that it need not be held in registers meanwhile.
+// time, so that it need not be held in registers meanwhile. (t0 < 256, and token strides below 2^22 by the
+// host's check, so their products are 24-bit ones.)
 struct Lane {
   int cg, ts, nominal, c0, rows;
   uint32_t t0;
@@ -387,8 +388,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
   const auto rx = segment_buffer<T>(a.x, p.b * a.xb + tseg * a.xt, a.xt, trows, a.C);
   {
     vec_t<T, VEC> f[L];
-    load_slice<T, VEC, L>(rf, q.t0 * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
-    load_slice<T, VEC, L>(rx, q.t0 * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
+    load_slice<T, VEC, L>(rf, __umul24(q.t0, (uint32_t)a.ft) + c0, (uint32_t)a.ft, f);
+    load_slice<T, VEC, L>(rx, __umul24(q.t0, (uint32_t)a.xt) + c0, (uint32_t)a.xt, x);
     if (p.u == 0 && a.state_in && threadIdx.x < CT && group < a.C)
       h0 = a.state_in[(int64_t)p.b * a.C + c];
     slice_gates<T, VEC, L>(f, q.rows, trows < SEG, v);
@@ -453,7 +454,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_kernel(RecurArgs a) {
   // read for that one's channels may be their final one already, so it stores its own channels alone.
   const bool crossing = VEC > 1 && p.tile * CT + VEC > a.C;
   auto store = [&](const Lane& k, int l, const float(&h)[VEC]) {
-    const uint32_t at = (k.t0 * (uint32_t)a.C + k.c0 + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
+    const uint32_t at = (__umul24(k.t0, (uint32_t)a.C) + k.c0 + (uint32_t)l * (uint32_t)a.C) * (uint32_t)sizeof(T);
     if (!crossing) {
       buffer_store_vec<T, VEC>(rh, at, h);
     } else {
@@ -524,9 +525,9 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
     const auto rf = segment_buffer<T>(a.f, p.b * a.fb + tseg * a.ft, a.ft, trows, a.C);
     const auto rx = segment_buffer<T>(a.x, p.b * a.xb + tseg * a.xt, a.xt, trows, a.C);
     const auto rd = segment_buffer<T>(a.dh, dense, a.C, trows, a.C);
-    load_slice<T, VEC, L>(rf, q.t0 * (uint32_t)a.ft + c0, (uint32_t)a.ft, f);
-    load_slice<T, VEC, L>(rx, q.t0 * (uint32_t)a.xt + c0, (uint32_t)a.xt, x);
-    load_slice<T, VEC, L>(rd, q.t0 * (uint32_t)a.C + c0, (uint32_t)a.C, dh);
+    load_slice<T, VEC, L>(rf, __umul24(q.t0, (uint32_t)a.ft) + c0, (uint32_t)a.ft, f);
+    load_slice<T, VEC, L>(rx, __umul24(q.t0, (uint32_t)a.xt) + c0, (uint32_t)a.xt, x);
+    load_slice<T, VEC, L>(rd, __umul24(q.t0, (uint32_t)a.C) + c0, (uint32_t)a.C, dh);
     if (real && threadIdx.x < 2 * CT) {
       if (threadIdx.x >= CT)
         from = a.carry[((int64_t)p.b * a.S + s) * a.C + c];
@@ -583,42 +584,28 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
   }
   lds_barrier();
   if (q.nominal >= a.C) return;
-  const uint32_t first = q.t0 * (uint32_t)a.C + c0;
-  float d[L][VEC], h[VEC];  // h_{t-1} - x, or h_{t-1}
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    h[i] = sH[ts][cg * VEC + i];
-#pragma unroll
-    for (int l = 0; l < L; ++l) {
-      const float xv = (float)x[l][i];
-      d[l][i] = COMP ? h[i] - xv : h[i];
-      if (l < L - 1) h[i] = advance<COMP>(v[l][i], sign_of(v[l][i]), h[i], xv);
-    }
-  }
-  if (__builtin_expect(!all_finite(h), 0)) {
-    const Again<VEC, L> g(v);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      h[i] = sH[ts][cg * VEC + i];
-#pragma unroll
-      for (int l = 0; l < L; ++l) {
-        const float xv = (float)x[l][i];
-        d[l][i] = COMP ? h[i] - xv : h[i];
-        h[i] = advance_ieee<COMP>(g.v[l][i], h[i], xv);
-      }
-    }
-  }
+  const uint32_t first = __umul24(q.t0, (uint32_t)a.C) + c0;
   const auto rdx = segment_buffer<T>(a.h, dense, a.C, trows, a.C);
   const auto rdf = segment_buffer<T>(a.df, dense, a.C, trows, a.C);
-  // runs and stores the slice; whether the gradient that leaves it is finite
+  // runs the slice forward for its states and backward for the gradients, and stores them; whether both
+  // came out finite
   auto run = [&](auto ieee, const float(&v)[L][VEC]) {
     constexpr bool IEEE = decltype(ieee)::value;
-    float r[VEC];
+    float d[L][VEC], h[VEC], r[VEC];  // d: h_{t-1} - x, or h_{t-1}
+    uint32_t m[L][VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
       const int c = cg * VEC + i;
+      h[i] = sH[ts][c];
       r[i] = IEEE ? run_end(sR[ts][c], rin[c], sG[ts][c], (zeros[c] >> ts >> 1) != 0)
                   : fmaf(sR[ts][c], rin[c], sG[ts][c]);
+#pragma unroll
+      for (int l = 0; l < L; ++l) {
+        const float w = v[l][i], xv = (float)x[l][i];
+        m[l][i] = sign_of(w);
+        d[l][i] = COMP ? h[i] - xv : h[i];
+        if (l < L - 1) h[i] = IEEE ? advance_ieee<COMP>(w, h[i], xv) : advance<COMP>(w, m[l][i], h[i], xv);
+      }
     }
 #pragma unroll
     for (int l = L - 1; l >= 0; --l) {
@@ -626,9 +613,8 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         const float w = v[l][i], g = (float)dh[l][i] + r[i];
-        const uint32_t m = sign_of(w);
-        r[i] = IEEE ? times_gamma_ieee(w, g) : times_gamma(w, m, g);
-        dx[i] = !COMP ? g : IEEE ? times_omg_ieee(w, g) : times_omg(w, m, g);
+        r[i] = IEEE ? times_gamma_ieee(w, g) : times_gamma(w, m[l][i], g);
+        dx[i] = !COMP ? g : IEEE ? times_omg_ieee(w, g) : times_omg(w, m[l][i], g);
         // gamma (1 - gamma) = s (1 - s) for either sign of f
         df[i] = fmaf(-w, w, fabsf(w)) * (g * d[l][i]);
       }
@@ -636,7 +622,7 @@ __global__ __launch_bounds__(S::NT, S::WAVES) void recur_bwd_kernel(RecurArgs a)
       buffer_store_vec<T, VEC>(rdx, off, dx);
       buffer_store_vec<T, VEC>(rdf, off, df);
     }
-    return all_finite(r);
+    return all_finite(h) && all_finite(r);
   };
   if (__builtin_expect(!run(std::false_type(), v), 0)) run(std::true_type(), Again<VEC, L>(v).v);
 }
@@ -648,7 +634,7 @@ __global__ __launch_bounds__(256) void recur_pass_kernel(const float* in, float*
 }
 
 // One token: VEC channels per thread, the row's last group as in the scans (each channel is stored by
-// its owner alone: the state is updated in place). 8192 sequences of 4096 channels in bf16 81 us (5.8
+// its owner alone: the state is updated in place). 8192 sequences of 4096 channels in bf16 85 us (5.5
 // TB/s); 256 of 1024 3.0 us, where any kernel takes 2.
 template <typename T, int VEC, bool COMP>
 __global__ __launch_bounds__(256) void recur_step_kernel(RecurArgs a) {
