@@ -13,7 +13,9 @@ Tensors are bfloat16 or float32 device tensors; weights, scales, states and thei
 float32. ``x``, ``gate``, ``f``, ``y`` and the residual stream may be slices of wider rows (the
 halves of a fused projection, say); everything else is dense. Work is enqueued on ``stream``
 (default: the current stream of the tensors' device); with another stream the caller orders it
-after the inputs' producers and before the outputs' readers.
+after the inputs' producers and before the outputs' readers. Results are plain tensors without an
+autograd history: training calls the ``*_bwd`` functions (examples/block_stack.py wraps them in
+autograd functions).
 """
 from __future__ import annotations
 
