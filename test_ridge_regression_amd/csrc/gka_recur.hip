@@ -27,8 +27,9 @@
 // so in them. A slice whose end is not finite is therefore run again, each step that is not finite in the
 // definition's form; finite channels keep their bits. A product of gates that underflows is kept above
 // zero, since an infinite state survives it, while a gate of zero times infinity is NaN. The checks cost a
-// finite call nothing to 2 % (8 sequences of 2048 steps by 1024 channels, slices of wider rows: 23.4 us
-// with them and 22.9 without).
+// finite call nothing to 2 % (8 sequences of 2048 steps by 1024 channels, slices of wider rows: 23.2 us
+// with them and 22.9 without), gates of zero in every slice up to 4 %, infinite states throughout 46 to
+// 69 % forward and 8 to 21 % backward.
 //
 // Measured (bf16): 4 sequences of 8192 steps by 2048 channels 90 us forward (4.5 TB/s) and 134 us
 // backward (5.0 TB/s); one of 131072 steps by 1024 channels 180 us (4.5 TB/s) and 316 us (4.3 TB/s).

@@ -167,3 +167,21 @@ def test_precision_of_the_smaller_sigmoid():
     want = np.exp(f) / (1.0 + np.exp(f))
     units = np.abs(got / want - 1.0) / 2.0 ** -24
     assert (units <= 6 + 1.25 * np.abs(f)).all(), units.max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,T,C", [(1, 100000, 16), (2, 50001, 70)])
+def test_hundreds_of_segments_repeat_bit_for_bit(B, T, C, dtype):
+    """Whichever words a segment's look-back finds, the chain of operations is the same."""
+    log(f"recur long chains {B}x{T}x{C} {dtype}")
+    rng = np.random.default_rng(T)
+    x, f, dh = (on_gpu(rng.standard_normal((B, T, C)) + m, dtype) for m in (0.0, 3.0, 0.0))
+    s0, ds = (on_gpu(rng.standard_normal((B, C)), "fp32") for _ in range(2))
+
+    def run():
+        st = s0.clone()
+        h, carry = block.recur(x, f, state=st, return_carry=True)
+        return (h, st, *block.recur_bwd(x, f, dh, carry, dstate=ds))
+    first = run()
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(run(), first))
